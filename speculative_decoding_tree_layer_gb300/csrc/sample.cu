@@ -982,7 +982,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampleArg
         const float c = sc.ch, range = mx - float_of(key_min);
         bn.scale = c * ((kBins - 1) / kOctaves);
         if (range > 0.0f && range < INFINITY) bn.scale = fmaxf(bn.scale, (kBins - 1) / range);
-        bn.scale = fminf(bn.scale, 3e38f);
+        // (four times it is finite: the count and the later passes bin alike)
+        bn.scale = fminf(bn.scale, 0x1p125f);
         const bool cut_p = top_p < 1.0f;
         // The bin of the last wanted maximum and what min_p leaves of it.
         auto cut_min_p = [&](int b_end) {
