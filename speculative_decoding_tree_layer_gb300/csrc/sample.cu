@@ -1439,18 +1439,22 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampleArg
         for (int i = i0; i < i1; ++i) n += key_of(xw[i]) == keep.key;
         ties = sh.xchg[par ^ 1][0][0] + block_exclusive32(sh, n, sum);
     }
-    auto token_mass = [&](int i, u64& rk) -> u64 {
+    auto token_mass = [&](int i, u64& rk, bool& kept) -> u64 {
         const uint32_t key = key_of(xw[i]);
-        if (key < keep.key || (key == keep.key && rk++ >= keep.ties)) return 0;
-        const u64 w = mass_of(xw[i], sc, sh.tab);
+        kept = key > keep.key || (key == keep.key && rk++ < keep.ties);
+        const u64 w = kept ? mass_of(xw[i], sc, sh.tab) : 0;
         return w >= w_min ? w : 0;
     };
+    // A kept token may have a mass (above 2^-46, as mass_pair2 has it) and still less
+    // than half a unit, and all that its warp holds may be such.
+    auto has_mass = [&](float x) { return x == sc.mx || (x - sc.mx) * sc.ch > -46.0f; };
     u64 mine_sum = 0, rk = ties, all_sum;
     int last = -1;
+    bool kept;
     for (int i = i0; i < i1; ++i) {
-        const u64 w = token_mass(i, rk);
+        const u64 w = token_mass(i, rk, kept);
         mine_sum += w;
-        if (w) last = i;
+        if (w || (kept && w_min == 0 && has_mass(xw[i]))) last = i;
     }
     u64 run = sh.pick + block_exclusive(sh, mine_sum, all_sum);
     const int first_hit = c0 + (int)w_hit * w_len;
@@ -1458,13 +1462,14 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampleArg
         rk = ties;
         int i = i0;
         for (; i < i1 - 1; ++i) {
-            run += token_mass(i, rk);
+            run += token_mass(i, rk, kept);
             if (run > draw) break;
         }
         store(first_hit + i, xw[i], total);
     }
     // The warp's sum was rounded per lane, these per token: a draw within those
-    // few units of its end belongs to its last token.
+    // few units of its end belongs to its last token that has a mass (there is one:
+    // the warp's sum is not zero).
     if (sh.pick + all_sum <= draw) {
         const int t = __reduce_max_sync(0xffffffffu, last);
         if (lane == 0) sh.least[warp] = (uint32_t)(t + 1);
