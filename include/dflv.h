@@ -566,7 +566,10 @@ typedef struct {
  * A sequence whose pages would exceed the row (or with a length out of
  * range), or whose demand added to that of the sequences before it exceeds
  * n_free, raises DFLV_DEV_CAPACITY, takes nothing and gets slots -1; every
- * later sequence that needs pages is refused with it in the second case. */
+ * later sequence that needs pages is refused with it in the second case.  A
+ * page id outside the pool, off the free list or of a held page that new tokens
+ * lie in, raises DFLV_DEV_PAGE: it goes to the table like the others, and the
+ * tokens of its page get slots -1. */
 dflv_status dflv_block_tables_grow(const dflv_pages_desc* desc, const int32_t* n_past, const int32_t* n_new,
                                    int32_t* n_held, const int32_t* free_list, int32_t* n_free, int32_t* table,
                                    int32_t* slots, int32_t* status_dev, dflv_stream_t stream);

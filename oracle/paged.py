@@ -11,7 +11,8 @@ DEV_TOPOLOGY, DEV_CAPACITY, DEV_PATH, DEV_PAGE, DEV_SAMPLE = 1, 2, 4, 16, 32
 
 
 def tables_grow(n_past, n_new, n_held, free_list, n_free, table, page, N_max):
-    """Returns (n_held, n_free, table, slots, status)."""
+    """Returns (n_held, n_free, table, slots, status).  The pool has as many pages
+    as free_list has places."""
     B, width = table.shape
     n_held, table = n_held.copy(), table.copy()
     slots = np.full((B, N_max), -1, np.int32)
@@ -29,11 +30,16 @@ def tables_grow(n_past, n_new, n_held, free_list, n_free, table, page, N_max):
             continue
         for t in range(held, held + more):
             table[b, t] = free_list[n_free - 1 - taken]
+            if not 0 <= table[b, t] < len(free_list):
+                status |= DEV_PAGE
             taken += 1
         n_held[b] = held + more
         for i in range(new):
             t = past + i
-            slots[b, i] = table[b, t // page] * page + t % page
+            if 0 <= table[b, t // page] < len(free_list):
+                slots[b, i] = table[b, t // page] * page + t % page
+            else:
+                status |= DEV_PAGE
     return n_held, n_free - taken, table, slots, status
 
 

@@ -80,6 +80,9 @@ DFLV_DEVINL int release_back(const PageTableArgs& a, int b, bool& bad) {
     return bad ? 0 : held - keep;
 }
 
+DFLV_DEVINL bool in_pool(const PageTableArgs& a, int id) { return (unsigned)id < (unsigned)a.n_pages; }
+constexpr int kNoSlots = -(1 << 30);  // negative with any place in a page added
+
 DFLV_DEVINL int free_count(const PageTableArgs& a) {
     const int f = *a.n_free;
     return f < 0 || f > a.n_pages ? 0 : f;
@@ -186,7 +189,10 @@ __global__ void __launch_bounds__(kTabThreads) tables_grow_kernel(const PageTabl
         for_rows(nb, [&](int s, int first, int step) {
             int32_t* row = a.table + (size_t)(b0 + s) * a.max_pages + held_s[s];
             const int32_t* top = a.free_list + (n_free - 1 - start_s[s]);
-            copy_pages(first, step, more_s[s], [&](int t) { return top[-t]; }, [&](int t, int id) { row[t] = id; });
+            copy_pages(first, step, more_s[s], [&](int t) { return top[-t]; }, [&](int t, int id) {
+                if (!in_pool(a, id)) raise_status(a.status, DFLV_DEV_PAGE);
+                row[t] = id;
+            });
         });
     const int shift = a.page_shift, mask = a.page - 1;
     const int i0 = blockIdx.y * kSlotChunk, i1 = min(a.N_max, i0 + kSlotChunk), w = i1 - i0;
@@ -195,6 +201,12 @@ __global__ void __launch_bounds__(kTabThreads) tables_grow_kernel(const PageTabl
         const int32_t* at = q < held_s[s] ? a.table + ((size_t)(b0 + s) * a.max_pages + q)
                                           : a.free_list + (n_free - 1 - (start_s[s] + q - held_s[s]));
         return *at;
+    };
+    // An id outside the pool gives no slots: shifted, it could name a slot of any page.
+    auto first_slot = [&](int id) {
+        if (in_pool(a, id)) return id << shift;
+        raise_status(a.status, DFLV_DEV_PAGE);
+        return kNoSlots;
     };
     if ((a.N_max & 3) == 0 && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
         // Four slots a thread and one 16-byte store: `here` of them lie in one
@@ -223,17 +235,18 @@ __global__ void __launch_bounds__(kTabThreads) tables_grow_kernel(const PageTabl
             for (int u = 0; u < U; ++u) {
                 if (e0 + u * kTabThreads >= all) break;
                 const int off = (past_s[s[u]] + i[u]) & mask, here = a.page - off, left = new_s[s[u]] - i[u];
-                const int x0 = (first[u] << shift) + off, x1 = (second[u] << shift) - here;
+                const int x0 = first_slot(first[u]) + off, x1 = first_slot(second[u]) - here;
                 int x[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = k < left ? (k < here ? x0 : x1) + k : -1;
+                for (int k = 0; k < 4; ++k) x[k] = k < left ? max((k < here ? x0 : x1) + k, -1) : -1;
                 *reinterpret_cast<int4*>(a.slots + (size_t)(b0 + s[u]) * a.N_max + i[u]) = make_int4(x[0], x[1], x[2], x[3]);
             }
         }
     } else {
         for (int e = tid; e < nb * w; e += kTabThreads) {
             const int s = e / w, i = i0 + (e - s * w), t = past_s[s] + i;
-            a.slots[(size_t)(b0 + s) * a.N_max + i] = i < new_s[s] ? (page_of(s, t >> shift) << shift) | (t & mask) : -1;
+            a.slots[(size_t)(b0 + s) * a.N_max + i] =
+                i < new_s[s] ? max(first_slot(page_of(s, t >> shift)) + (t & mask), -1) : -1;
         }
     }
     if (kFuse) {
@@ -277,7 +290,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_release_kernel(const PageT
         for_rows(nb, [&](int s, int first, int step) {
             const int32_t* row = a.table + (size_t)(b0 + s) * a.max_pages + keep_s[s];
             copy_pages(first, step, back_s[s], [&](int t) { return row[t]; }, [&](int t, int id) {
-                if ((unsigned)id >= (unsigned)a.n_pages) raise_status(a.status, DFLV_DEV_PAGE);
+                if (!in_pool(a, id)) raise_status(a.status, DFLV_DEV_PAGE);
                 *(top - (start_s[s] + t)) = id;
             });
         });

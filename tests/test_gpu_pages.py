@@ -216,3 +216,32 @@ def test_commit_leaves_a_bad_sequence_alone(dflv, path, plen, slot, bits):
                                          st))
     assert int(st) == bits and int(past) == 7
     assert np.array_equal(host(dk).view(np.uint16), k) and np.array_equal(host(dv).view(np.uint16), v)
+
+
+@pytest.mark.parametrize("B,N", [(3, 40), (3, 41), (300, 44), (300, 33)])
+@pytest.mark.parametrize("bad", [-1, -(1 << 31), 0, 3, 1 << 27, (1 << 28) + 1, (1 << 31) - 1])
+def test_grow_gives_no_slots_in_pages_outside_the_pool(dflv, B, N, bad):
+    # damaged ids in held pages and in the free list, some of which name a page of
+    # the pool once they are shifted to a slot (ids 0 and 3 stand for one past it)
+    rng = np.random.default_rng(B + N)
+    page, width = 16, 8
+    past = rng.integers(1, 40, B).astype(np.int32)
+    new = rng.integers(1, N + 1, B).astype(np.int32)
+    table, held, free, n_free = pool(rng, past, width, page, int((-(-new // page) + 1).sum()))
+    bad = len(free) + bad if bad in (0, 3) else bad
+    for b in range(0, B, 3):
+        table[b, held[b] - 1] = bad
+    free[n_free - 1 - rng.integers(0, n_free // 2, max(1, B // 8))] = bad
+    rh, rf, rt, rs, st = paged.tables_grow(past, new, held, free, n_free, table, page, N)
+    assert st == paged.DEV_PAGE
+    _, d = grow(dflv, past, new, held, free, n_free, table, page, N)
+    assert int(d["st"]) == st
+    for name, ref in (("table", rt), ("slots", rs), ("held", rh), ("n_free", [rf]), ("free", free)):
+        assert np.array_equal(host(d[name]), ref), name
+    # a damaged page that no new token lies in is not looked at
+    table[:, 0] = bad
+    past = (held * page).astype(np.int32)
+    free[:n_free] = np.arange(n_free)
+    rh, rf, rt, rs, st = paged.tables_grow(past, new, held, free, n_free, table, page, N)
+    _, d = grow(dflv, past, new, held, free, n_free, table, page, N)
+    assert st == 0 and int(d["st"]) == 0 and np.array_equal(host(d["slots"]), rs)
