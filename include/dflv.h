@@ -673,10 +673,11 @@ typedef struct {
  * for the product with the values.  What masked places hold, NaN and
  * infinities included, does not reach the output.
  * An n_nodes outside [0, N_max] or a malformed parent array raises
- * DFLV_DEV_TOPOLOGY; a negative n_past, tokens past the table row or a
- * prefix_len outside the prefix table DFLV_DEV_CAPACITY (a sequence so marked
- * takes no part, a prefix so marked counts as empty); a page id outside the
- * pool DFLV_DEV_PAGE (page 0 is read in its place).  Tables that name the same
+ * DFLV_DEV_TOPOLOGY; a negative n_past or tokens past the table row raise
+ * DFLV_DEV_CAPACITY.  A sequence so marked takes no part: its rows of out are
+ * not written.  A prefix_len outside the prefix table raises DFLV_DEV_CAPACITY
+ * and counts as no prefix; a page id outside the pool raises DFLV_DEV_PAGE,
+ * and page 0 is read in its place.  Tables that name the same
  * pages so often that the batch's 64-key tiles times its row tiles pass 2^31
  * raise DFLV_DEV_CAPACITY, and nothing is computed. */
 dflv_status dflv_prefix_attn_verify(const dflv_prefix_attn_desc* desc, const int32_t* prefix_table,

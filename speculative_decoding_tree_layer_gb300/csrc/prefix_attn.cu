@@ -424,6 +424,10 @@ DFLV_DEVINL void st16_nowait(uint32_t taddr, const uint32_t (&v)[16]) {
         : "memory");
 }
 
+// In the place of a row's sum where the segment reaches a malformed tree, as the
+// last one of every row of that sequence does: the join writes nothing for it.
+constexpr float kMalformed = -1.0f;
+
 constexpr int kMaxStages = 16;
 constexpr int kMaxBufs = 4;
 constexpr int kBadSlots = 16;  // segments the fix warp can be ahead of the softmax: fewer than half the stages + 1
@@ -853,6 +857,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             const unsigned long long* bad_nodes = &hd->bad[n_seg++ % kBadSlots];
             // ---- the row's ancestors, when the segment reaches the tree
             unsigned long long anc = 0;
+            bool malformed = false;
             if (n > 0 && (s.t0 + s.nt) * kKT > past) {
                 int* par = hd->par[warp];  // a copy per warp: no barrier between warps
                 __syncwarp();
@@ -860,11 +865,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     int p = x - 1;
                     if (a.parent) {
                         const int q = __ldg(a.parent + (size_t)s.b * a.N_max + x);
-                        if (x == 0 ? q != -1 : (q < 0 || q >= x)) raise_status(status, DFLV_DEV_TOPOLOGY);
+                        if (x == 0 ? q != -1 : (q < 0 || q >= x)) malformed = true;
                         else p = q;
                     }
                     par[x] = p;
                 }
+                malformed = __any_sync(0xffffffffu, malformed);
+                if (malformed && lane == 0) raise_status(status, DFLV_DEV_TOPOLOGY);
                 __syncwarp();
                 if (live)
                     for (int x = node; x >= 0; x = par[x]) anc |= 1ull << x;
@@ -1002,7 +1009,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 // one line
                 float2* ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(a.ws) + lay.off_ml) + seg0 + in_seg;
                 float* po = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + lay.off_o) + seg0 * D + in_seg;
-                if (live && (!kOne || grp == 0)) *ml = make_float2(m * c, l);
+                if (live && (!kOne || grp == 0)) *ml = make_float2(m * c, malformed ? kMalformed : l);
                 const unsigned long long bad = s.b < 0 ? 0ull : *bad_nodes & anc;
                 const int d0 = kOne ? grp * C::kOwnCols : 0;
                 if (kOne || grp < steps) {  // (a group without a tile has no O)
@@ -1138,6 +1145,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_attn_join_kernel(const
     const int part = kSplit == 1 ? 0 : warp;
     // A running maximum: (max, sum) and O are asked for together.
     float top = -INFINITY, sum = 0.0f, acc[E];
+    bool drop = false;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
     const int c0 = (kSplit == 1 ? blockIdx.z * kJoinWarps + warp : blockIdx.z) * E;
@@ -1156,6 +1164,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_attn_join_kernel(const
         }
         // (a sum of zero: nothing seen there, its O was not written)
         float next = top;
+#pragma unroll
+        for (int u = 0; u < U; ++u) drop |= x[u].y == kMalformed;
         bool use[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -1179,7 +1189,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_attn_join_kernel(const
         __shared__ float red[kSplit][E + 2][32];
 #pragma unroll
         for (int e = 0; e < E; ++e) red[warp][e][lane] = acc[e];
-        red[warp][E][lane] = sum;
+        red[warp][E][lane] = drop ? kMalformed : sum;
         red[warp][E + 1][lane] = top;
         __syncthreads();
         if (warp != 0) return;
@@ -1191,12 +1201,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_attn_join_kernel(const
 #pragma unroll
         for (int q = 0; q < kSplit; ++q) {
             const float l = red[q][E][lane], f = l == 0.0f ? 0.0f : ex2(red[q][E + 1][lane] - top);
+            drop |= l == kMalformed;
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] = l == 0.0f ? acc[e] : fmaf(f, red[q][e][lane], acc[e]);
             sum = l == 0.0f ? sum : fmaf(f, l, sum);
         }
     }
-    if (!live) return;
+    if (!live || drop) return;
     const float inv = 1.0f / sum;
     uint32_t out[E / 2];
 #pragma unroll

@@ -313,3 +313,32 @@ def test_results_do_not_depend_on_the_call(dflv):
         assert torch.equal(out, fresh)
         c.prefix, c.n = full, keep
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("shape", [(2, 4, 4, 2, 64, 16, 40, [20, 20], [4, 3]), (2, 4, 6, 2, 128, 16, 300, [0, 70], [4, 4]),
+                                   (3, 40, 12, 2, 256, 64, 0, [130, 9, 60], [33, 40, 40]),
+                                   (700, 3, 2, 1, 64, 16, 33, [5] * 700, [3] * 700)])
+def test_a_malformed_tree_takes_no_part(dflv, shape):
+    B, N, Hq, Hkv, D, page, prefix, past, n = shape
+    c = Case(14, B, N, Hq, Hkv, D, page, "bf16", prefix, past, n)
+    ref = c.oracle()
+    good = c.parent.copy()
+    for b in {0, B - 1, B // 2}:
+        last = int(c.n[b]) - 1
+        for at, value in ((0, 0), (0, -2), (1, -1), (1, 1), (last, last), (last, 1 << 30)):
+            par = good.copy()
+            par[b, at] = value
+            out, st = c.run(dflv, parent=par)
+            assert st == dflv.DFLV_DEV_TOPOLOGY
+            assert (out[b] == -7).all()
+            n0, c.n = c.n, c.n.copy()
+            c.n[b] = 0
+            c.compare(out, ref)
+            c.n = n0
+    # what stands behind a tree's nodes, or in a sequence without any, is not looked at
+    par = good.copy()
+    for b in range(B):
+        par[b, int(c.n[b]):] = 1 << 20
+    out, st = c.run(dflv, parent=par)
+    assert st == 0
+    c.compare(out, ref)
