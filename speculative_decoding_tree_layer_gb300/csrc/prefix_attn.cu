@@ -764,8 +764,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         // ------------------------------------------------ softmax
         const int grp = warp >> 2, row = tid & 127;
         const uint32_t lane_base = (uint32_t)(warp & 3) * 32u << 16;
-        // (a scale of zero still has to mask: -infinity x 0 is NaN)
-        const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+        // (a scale of zero still has to mask, as -infinity x 0 is NaN: with the
+        // smallest float no finite score comes to more than 2^-21)
+        const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 0x1p-149f);
         const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;  // q negated for a negative scale
         // fp16 weights are scaled by 2^6 (they stay below 2^14): fewer of them
         // are subnormal.  Sums and O carry the factor alike.

@@ -342,3 +342,50 @@ def test_a_malformed_tree_takes_no_part(dflv, shape):
     out, st = c.run(dflv, parent=par)
     assert st == 0
     c.compare(out, ref)
+
+
+class Scaled(Case):
+    scale = 0.0
+
+    def desc(self, dflv, q_stride=0):
+        d = super().desc(dflv, q_stride)
+        d.scale = self.scale
+        return d
+
+    def oracle(self, n=None):
+        f = lambda x: x.double().numpy()  # noqa: E731
+        with np.errstate(invalid="ignore", over="ignore"):
+            return paged.prefix_attn(self.ptab - self.first, self.prefix, self.tab - self.first, self.parent,
+                                     self.n if n is None else n, self.past, f(self.q), f(self.k), f(self.v),
+                                     float(np.float32(self.scale)))
+
+
+SCALED = [(3, 5, 6, 2, 64, 16, 130, [20, 63, 0], [5, 1, 4]), (2, 40, 12, 2, 128, 16, 200, [40, 61], [40, 30]),
+          (3, 22, 24, 4, 256, 64, 300, [100, 0, 42], [22, 5, 0])]
+
+
+@pytest.mark.parametrize("shape", SCALED)
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [-1.0, -0.25, 0.0, -0.0, 1e-20, -1e-35, 2.0 ** -149])
+def test_scales_of_either_sign_and_none(dflv, shape, kind, scale):
+    # (-1 and -0.25: as parts of 1 / sqrt(D), for which the tolerance is derived)
+    B, N, Hq, Hkv, D, page, prefix, past, n = shape
+    c = Scaled(15, B, N, Hq, Hkv, D, page, kind, prefix, past, n)
+    c.scale = scale / math.sqrt(D) if scale <= -0.25 else scale
+    out, st = c.run(dflv)
+    assert st == 0
+    c.compare(out)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("scale,factor", [(0.0, 2.0 ** 100), (1e-35, 2.0 ** 110), (-2.0 ** -120, 2.0 ** 114)])
+def test_scales_that_undo_large_scores(dflv, D, scale, factor):
+    # products of queries and keys of up to 2^120: none of their size is left in
+    # the weights
+    c = Scaled(16, 3, 5, 6, 2, D, 16, "bf16", 130, [20, 63, 0], [5, 1, 4])
+    c.q = (c.q.float() * (factor / 2.0 ** 60)).bfloat16()
+    c.k = torch.where(torch.isfinite(c.k), c.k.float() * 2.0 ** 60, c.k.float()).bfloat16()
+    c.scale = scale
+    out, st = c.run(dflv)
+    assert st == 0
+    c.compare(out)
