@@ -389,3 +389,11 @@ def test_scales_that_undo_large_scores(dflv, D, scale, factor):
     out, st = c.run(dflv)
     assert st == 0
     c.compare(out)
+
+
+def test_equal_scores_and_their_status(dflv):
+    c = Case(17, 2, 3, 4, 2, 64, 16, "bf16", 300, [100, 5], [3, 3])
+    c.k[:] = 0.5                     # all scores of a row equal: the mean of the values
+    out, st = c.run(dflv)
+    assert st == 0
+    c.compare(out)
