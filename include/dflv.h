@@ -640,7 +640,7 @@ dflv_status dflv_paged_kv_commit(const dflv_paged_kv_desc* desc, int32_t n_layer
  * of q (0 = Hq * D; a multiple of 8, at least Hq * D).
  * Supported: 1 <= N_max <= 64, B <= 1024, Hq <= 1024, Hq / Hkv <= 64, D in
  * {64, 128, 256}, page in {16, 32, 64, 128}, type DFLV_KV_BF16 or DFLV_KV_F16,
- * a finite scale, max_pages * page and max_prefix_pages * page below 2^30,
+ * |scale| <= 2^127, max_pages * page and max_prefix_pages * page below 2^30,
  * n_pages * page below 2^31. */
 typedef struct {
     int32_t B, N_max, Hq, Hkv, D, page, n_pages, max_pages, max_prefix_pages;

@@ -507,6 +507,7 @@ dflv_status check_prefix_attn_desc(const dflv_prefix_attn_desc* d) {
     if (d->Hq % d->Hkv != 0 || !(d->scale - d->scale == 0.0f)) return DFLV_ERR_INVALID_ARG;  // (not finite)
     if (d->type != DFLV_KV_BF16 && d->type != DFLV_KV_F16) return DFLV_ERR_UNSUPPORTED;
     if (d->D != 64 && d->D != 128 && d->D != 256) return DFLV_ERR_UNSUPPORTED;
+    if (d->scale > 0x1p127f || d->scale < -0x1p127f) return DFLV_ERR_UNSUPPORTED;  // times log2(e): not finite
     if (d->N_max > 64 || d->B > 1024 || d->Hq / d->Hkv > 64 || d->Hq > 1024 || page_shift_of(d->page) < 0)
         return DFLV_ERR_UNSUPPORTED;
     if ((long long)d->max_pages * d->page >= (1ll << 30) || (long long)d->max_prefix_pages * d->page >= (1ll << 30) ||

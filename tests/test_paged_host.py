@@ -242,3 +242,10 @@ def test_oracle_sampling():
     assert draw(0.9, T=0.0) == 1
     assert paged.sample_row(x, -1.0, 0, 1.0, 0.0, 0.5)[3] == paged.DEV_SAMPLE
     assert paged.sample_row([-math.inf] * 4, 1.0, 0, 1.0, 0.0, 0.5)[::3] == (0, paged.DEV_SAMPLE)
+
+
+@pytest.mark.parametrize("scale,code", [(3e38, UNS), (-3e38, UNS), (2.0 ** 127, CAP), (-(2.0 ** 127), CAP), (0.0, CAP)])
+def test_attn_scales(scale, code):
+    # beyond 2^127 the scale times log2(e) is not finite (CAP: what comes after the
+    # descriptor, a workspace of no bytes)
+    assert attn(at(scale=scale), ws_bytes=0) == code
