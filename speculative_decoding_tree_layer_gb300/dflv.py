@@ -355,7 +355,7 @@ def _rows(x, dtypes, B, N, inner, stride, dev):
             raise _Refused
         return x.data_ptr()
     shape, st = x.shape, x.stride()
-    if len(shape) < 3 or shape[0] < B or shape[1] != N or x[0, 0].numel() != inner or \
+    if len(shape) < 3 or not x.numel() or shape[0] < B or shape[1] != N or x[0, 0].numel() != inner or \
             not x[0, 0].is_contiguous() or (N > 1 and st[1] != stride) or (B > 1 and st[0] != N * stride):
         raise _Refused
     return x.data_ptr()

@@ -249,3 +249,12 @@ def test_attn_scales(scale, code):
     # beyond 2^127 the scale times log2(e) is not finite (CAP: what comes after the
     # descriptor, a workspace of no bytes)
     assert attn(at(scale=scale), ws_bytes=0) == code
+
+
+@pytest.mark.parametrize("shape", [(0, 4, 2, 64), (2, 0, 2, 64), (0, 0, 2, 64)])
+def test_rows_of_an_empty_tensor_are_refused(shape):
+    # with a stride of their own, whatever the descriptor says
+    x = torch.empty(shape, dtype=torch.bfloat16)
+    for B, N in ((0, 0), shape[:2], (2, 4)):
+        with pytest.raises(dflv._Refused):
+            dflv._rows(x, (torch.bfloat16,), B, N, 128, 256, x.get_device())
