@@ -185,12 +185,13 @@ __global__ void __launch_bounds__(kTabThreads) tables_grow_kernel(const PageTabl
             raise_status(a.status, DFLV_DEV_CAPACITY);
     }
     __syncthreads();
+    bool bad_id = false;
     if (blockIdx.y == 0)
         for_rows(nb, [&](int s, int first, int step) {
             int32_t* row = a.table + (size_t)(b0 + s) * a.max_pages + held_s[s];
             const int32_t* top = a.free_list + (n_free - 1 - start_s[s]);
             copy_pages(first, step, more_s[s], [&](int t) { return top[-t]; }, [&](int t, int id) {
-                if (!in_pool(a, id)) raise_status(a.status, DFLV_DEV_PAGE);
+                bad_id |= !in_pool(a, id);
                 row[t] = id;
             });
         });
@@ -204,9 +205,9 @@ __global__ void __launch_bounds__(kTabThreads) tables_grow_kernel(const PageTabl
     };
     // An id outside the pool gives no slots: shifted, it could name a slot of any page.
     auto first_slot = [&](int id) {
-        if (in_pool(a, id)) return id << shift;
-        raise_status(a.status, DFLV_DEV_PAGE);
-        return kNoSlots;
+        const bool ok = in_pool(a, id);
+        bad_id |= !ok;
+        return ok ? id << shift : kNoSlots;
     };
     if ((a.N_max & 3) == 0 && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
         // Four slots a thread and one 16-byte store: `here` of them lie in one
@@ -249,6 +250,8 @@ __global__ void __launch_bounds__(kTabThreads) tables_grow_kernel(const PageTabl
                 i < new_s[s] ? max(first_slot(page_of(s, t >> shift)) + (t & mask), -1) : -1;
         }
     }
+    // (once a thread: raised where each is found, 1024 prompts take 17.1 us, not 16.4)
+    if (bad_id) raise_status(a.status, DFLV_DEV_PAGE);
     if (kFuse) {
         __syncthreads();
         update_counts<true>(a, red);
