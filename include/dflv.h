@@ -476,7 +476,7 @@ typedef enum { DFLV_LOGITS_F32 = 0, DFLV_LOGITS_BF16 = 1, DFLV_LOGITS_F16 = 2 } 
 
 /* Shape of a sampling call: B sequences of N_max rows (nodes), V logits a
  * row.  ld: elements between the starts of consecutive rows (0 = V).
- * Supported: 1 <= V <= 400000, B * N_max < 2^26, ld >= V. */
+ * Supported: 1 <= V <= 400000, B * N_max < 2^26, V <= ld <= 2^40. */
 typedef struct {
     int32_t B, N_max, V;
     dflv_logits_type type;
@@ -502,9 +502,10 @@ typedef struct {
  * 2^-127.  x_v - max x is taken in fp32: where it overflows, w_v is 0.
  * Out of range: temperature negative, infinite or NaN, top_p or min_p
  * negative or NaN, min_p above 1, u outside [0, 1) or NaN.  Such a row raises
- * DFLV_DEV_SAMPLE and gets its most likely token (logp 0), and so does a row
- * without any logit above -infinity (token 0, as dflv_accept_greedy), and a
- * row whose largest logit is +infinity draws among the tokens of that logit.
+ * DFLV_DEV_SAMPLE and gets its most likely token, logp 0.  A row without any
+ * logit above -infinity raises it too and gets token 0, as dflv_accept_greedy
+ * has it.  A row whose largest logit is +infinity draws among the tokens of
+ * that logit.
  *   logits [B][N_max][V] of the descriptor's type, rows ld apart, 16-byte
  *          aligned start (rows need not be)
  *   temperature, top_p, min_p [B] f32; top_k [B] int32: per sequence

@@ -10,11 +10,12 @@
 // CTA does the work), after every CTA has read them.
 //
 // A slot costs 4 bytes written, a page 4 bytes read and 4 written, a cache row is
-// read and written once.  Small calls are bound by the launch (8 sequences of 22
-// nodes: grow and release 12.5 us, the host's time for the two calls; the accepted
-// path of 16 layers 21 us, the host's too).  1024 prompts of 4096 tokens, grow and
-// release: 17 us for 20 MB, four launches that wait for one another.  Prompts of
-// 16 x 2048 tokens into the cache: 201 MB in 38.6 us, 5.2 TB/s.
+// read and written once.  Small calls are bound by the host and the launches (8
+// sequences of 22 nodes: grow and release 12 us, 7 of them on the GPU; the accepted
+// path of 16 layers 21 us, 4.5 of them on the GPU).  1024 prompts of 4096 tokens, grow
+// and release: 16.4 us for 20 MB, four launches that wait for one another (17 us in
+// a replayed graph too).  Prompts of 16 x 2048 tokens into the cache: 201 MB in 36.9
+// us, 5.4 TB/s.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -436,7 +437,7 @@ static cudaError_t launch_tables(const PageTableArgs& a, cudaStream_t stream) {
     // a second one pays for its own sums.
     const long long work = kGrow ? (long long)a.B * a.N_max : (long long)a.B * 256;
     long long want = work / 2048;
-    // (1024 sequences of 4096 new slots: grow and release take 17.0 us with two,
+    // (1024 sequences of 4096 new slots: grow and release take as long with two,
     // four or eight CTAs an SM)
     if (want > 2L * sms) want = 2L * sms;
     if (want > a.B) want = a.B;

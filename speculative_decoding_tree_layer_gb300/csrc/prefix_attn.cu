@@ -36,6 +36,12 @@
 //   * softmax warps (one thread per query row): online softmax with a lazily
 //     updated maximum (O is rescaled only when a row's maximum grows by more
 //     than 2^8), P rounded to the 16-bit type, sums in fp32 of the unrounded P.
+//     The rounding is what the product with V takes (its operands have one type,
+//     and V is 16-bit); a second product with the remainder of P would double that
+//     half of the matrix work.  Each weight is off by half a step of the type at
+//     most, in either direction, so their weighted mean of the values, itself
+//     rounded to the type, has 1.2 to 1.4 times the error of a result that is
+//     rounded once.
 // Head sizes 64 and 128 have room for two accumulators in tensor memory and
 // run two softmax groups: on two halves of the rows with the same key tiles
 // when a unit has more than 128 rows, else on the same rows with alternating
@@ -44,12 +50,13 @@
 //
 // What bounds it.  Many rows on a long prefix: the matrix products, which wait
 // for the softmax between a tile's two and for their operands from shared memory
-// (trees of 22 nodes, 16,384 shared tokens: 16 trees, 24/4 heads of 256, 95 us, 1.08
-// PFLOP/s; 64 trees, 32/8 heads of 128, 247 us, 1.14).  Single tokens: the latency
-// of a unit's start and end, some 8 K cycles a segment, of which half is hidden
-// (64 sequences of 8,192 shared and 512 to 1,024 own tokens, 32/8 heads of 128:
-// 60 us, of which the join 8, 220 MB at 3.7 TB/s).  A handful of sequences: plan,
-// first tiles, one segment and the join, one after the other (15 us).
+// (trees of 22 nodes, 16,384 shared tokens: 16 trees, 24/4 heads of 256, 106 us, 1.09
+// PFLOP/s; 64 trees, 32/8 heads of 128, 283 us, 1.03; 103 and 250 us where the keys
+// are in the L2).  Single tokens: the latency of a unit's start and end, some 8 K
+// cycles a segment, of which half is hidden (64 sequences of 8,192 shared and 512 to
+// 1,024 own tokens, 32/8 heads of 128: 69 us, this kernel 61 of them, 239 MB at 3.9
+// TB/s).  A handful of sequences: plan, first tiles, one segment and the join, one
+// after the other (16 us).  (Times without the host's, from a cold L2.)
 #include <cuda.h>
 
 #include <atomic>
@@ -66,14 +73,15 @@ constexpr int kKT = 64;          // keys per tile
 // Places on the line that a unit's query load and result store are worth, by
 // rows of a unit (R = 128: head size 256, else 256).  Where the CTAs get fewer
 // tiles than that each, a unit is better cut into segments than kept whole, and
-// the set-up counts as much as a CTA's tiles.  Measured, in us:
+// the set-up counts as much as a CTA's tiles.  Measured, in us, the keys in the L2:
 //   head size 128, places                                   5    8   12   16
-//     64 sequences of a token, 8,192 shared, 1,024 own     60   60   60   65
-//     their own tokens alone                               71   60   56   56
-//     64 trees of 22 nodes, 16,384 shared                 394  283  247  248
+//     64 sequences of a token, 8,192 shared, 1,024 own     62   60   62   65
+//     their own tokens alone                               55   55   56   56
+//     64 trees of 22 nodes, 16,384 shared                 394  285  250  248
 //   head size 256, places                                   4    8   12
-//     16 trees of 22 nodes, 16,384 shared, 2,048 own      116  112  110
-//     their shared tokens alone                           128   95   97
+//     16 trees of 22 nodes, 16,384 shared, 2,048 own      130  122  113
+//     their shared tokens alone                           154  103  105
+// (Head size 256 has 8: 12 gains 9 us on the one and loses 2 on the other.)
 template <int R>
 __host__ __device__ constexpr int most_setup() { return R == 128 ? 8 : 12; }
 constexpr int kMaxB = 1024;

@@ -22,9 +22,10 @@
 // What bounds it: one row, the exchanges between the CTAs (about 1.1 K cycles
 // each, and 3 to 5 K where they read each other's bins); many rows, the
 // instructions, as a mass takes about 30 and the loads are done after a third of
-// a row's time.  151,936 logits, in us, with 1 / 64 / 264 rows: argmax (T = 0) 4.3 /
-// 14.5 / 50, top-k 50 and top-p 0.9 9.9 / 28 / 98, no filter 10.9 / 35 / 125, min-p
-// 0.05 13 / 40 / 141, top-p 0.95 of a flat row (28,000 tokens kept) 30 / 93 / 326.
+// a row's time.  151,936 fp32 logits from a cold L2, in us without the host's time,
+// with 1 / 64 / 264 rows: argmax (T = 0) 5.4 / 17 / 52, top-k 50 and top-p 0.9 11.5 /
+// 29 / 99, no filter 12.3 / 38 / 125, min-p 0.05 15 / 42 / 140, top-p 0.95 alone 44 / 95
+// / 328.
 //
 // A token's mass e^{(x - max) / T} is computed to 2^-30 of itself as a pair of
 // floats, summed per thread in such pairs and from there on as 64-bit integers
@@ -741,6 +742,9 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampleArg
             }
         }
     } else {
+        // One token at a time, without the loads in flight above: three rows of four
+        // where V is odd.  64 rows of bf16, no filter: 24.0 us with 50,257 tokens, 15.0
+        // with 50,256; fp32 27.6 and 16.0.
         for (int i = lane; i < w_len; i += 32) xs[i] = i < n_own ? take(to_float<T>(row[i]), i) : -INFINITY;
     }
     // largest key, then lowest index
