@@ -546,7 +546,7 @@ dflv_status dflv_accept_sampled(const dflv_sample_desc* desc, const void* logits
  * page table[b][t / page], place t % page.  A shared prompt has a table of
  * its own (dflv_prefix_attn_verify); the sequences' tables hold only what
  * follows it.
- * Supported: page in {16, 32, 64, 128}; N_max <= 2^27; B * N_max,
+ * Supported: page in {16, 32, 64, 128}; B <= 2^20; N_max <= 2^27; B * N_max,
  * B * max_pages, max_pages * page and n_pages * page below 2^31. */
 typedef struct {
     int32_t B, N_max, page, n_pages;

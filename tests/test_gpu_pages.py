@@ -245,3 +245,24 @@ def test_grow_gives_no_slots_in_pages_outside_the_pool(dflv, B, N, bad):
     rh, rf, rt, rs, st = paged.tables_grow(past, new, held, free, n_free, table, page, N)
     _, d = grow(dflv, past, new, held, free, n_free, table, page, N)
     assert st == 0 and int(d["st"]) == 0 and np.array_equal(host(d["slots"]), rs)
+
+
+def test_as_many_sequences_as_there_may_be(dflv):
+    # 2^20 of them: three in four need a page, and the last ones get none
+    B, page = 1 << 20, 16
+    rng = np.random.default_rng(6)
+    new = (rng.random(B) < 0.75).astype(np.int32)
+    n_free = int(new.sum()) - 1000
+    free = rng.permutation(n_free + 5).astype(np.int32)
+    zero, table = np.zeros(B, np.int32), np.full((B, 1), -1, np.int32)
+    desc, d = grow(dflv, zero, new, zero, free, n_free, table, page, 1)
+    rank = np.cumsum(new) - new
+    served = (new > 0) & (rank < n_free)
+    ids = np.where(served, free[np.clip(n_free - 1 - rank, 0, None)], -1)
+    assert int(d["st"]) == dflv.DFLV_DEV_CAPACITY and int(d["n_free"]) == 0
+    assert np.array_equal(host(d["held"]), served) and np.array_equal(host(d["table"])[:, 0], ids)
+    assert np.array_equal(host(d["slots"])[:, 0], np.where(served, ids * page, -1))
+    d["st"].zero_()
+    dflv.check(dflv.dflv_block_tables_release(desc, dev(zero), d["held"], d["free"], d["n_free"], d["table"], d["st"]))
+    assert int(d["st"]) == 0 and int(d["n_free"]) == n_free and not host(d["held"]).any()
+    assert np.array_equal(host(d["free"]), free)

@@ -258,3 +258,11 @@ def test_rows_of_an_empty_tensor_are_refused(shape):
     for B, N in ((0, 0), shape[:2], (2, 4)):
         with pytest.raises(dflv._Refused):
             dflv._rows(x, (torch.bfloat16,), B, N, 128, 256, x.get_device())
+
+
+@pytest.mark.parametrize("call,first", [(grow, "n_past"), (release, "keep_len")])
+def test_tables_of_too_many_sequences_are_refused(call, first):
+    # whose sums would take the GPU minutes and more (BAD: the NULL that comes
+    # after the descriptor)
+    for B, code in ((1 << 20, BAD), ((1 << 20) + 1, UNS), (1 << 30, UNS)):
+        assert call(dflv.pages_desc(B, 1, 16, 8, 1), **{first: None}) == code
